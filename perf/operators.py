@@ -191,8 +191,13 @@ def _prepare_sparse(st, case, seed):
     st["q"] = _randn((B, case["Hq"], D), _gen(seed, 3)).to(torch.bfloat16)
     st["out"] = torch.empty_like(st["q"])
     st["blocks"] = torch.empty((B, H, case["blocks"]), dtype=torch.int32, device=DEV)
-    if own and case["kv"] != "fp8_e4m3_block":
-        return _fill(st, case, k, v, keep)
+    if own:
+        import compressed_decode_attention_fdms_b200 as fd
+        c = _cache(case, case["Hq"], D, case["kv"], 0)
+        fd.fdms_append_evict(c, 0, B, st["n"], T, k, v, keep)
+        fd.fdms_bounds_create(c)
+        st["cache"] = c
+        return st
     n = st["n"].long()[:, None, None]
     pos = torch.arange(T, device=DEV)[None, :, None]
     inside = pos < n
@@ -230,9 +235,6 @@ def _prepare_sparse(st, case, seed):
         # each sequence's last min(W, n) tokens, at its end
         at = torch.clamp(n[:, :, 0] - tail + torch.arange(tail, device=DEV)[None, :], min=0)
         st["ring_" + name] = torch.gather(r, 2, at[:, None, :, None].expand(-1, H, -1, D))
-    if own:
-        whole = torch.arange(room, device=DEV) < (length // BLOCK * BLOCK)[:, :, None]
-        return _fill(st, case, k, v, keep, (pick, whole, scaled))
     tail = st["ring_k"].shape[2]
     place = n[:, :, 0] - tail + torch.arange(tail, device=DEV)[None, :]
     st["ring_on"] = (place >= 0) & (place >= n[:, :, 0] - W)                # [B][tail]
@@ -241,39 +243,6 @@ def _prepare_sparse(st, case, seed):
     kb = scaled["k"][:, :, :nb * BLOCK].unflatten(2, (nb, BLOCK)) if nb else \
         scaled["k"][:, :, :0].reshape(B, H, 0, BLOCK, D)
     st["kmin"], st["kmax"] = kb.amin(3), kb.amax(3)
-    return st
-
-
-def _fill(st, case, k, v, keep, sealed=None):
-    """The cache of the calls, holding the values that the plain form holds.
-
-    torch divides by a number as a product with its reciprocal, so that the scales
-    above can be one unit off the cache's quotients, and an E4M3 code next to a
-    border can be another one. A cache with a scale per head is given the scales. A
-    cache with a scale per block is given, for the rows of its full blocks, the
-    values that the codes stand for (in bf16, 2^-9 off at most: they round to the
-    same codes again)."""
-    import compressed_decode_attention_fdms_b200 as fd
-    B, T, H, D = k.shape
-    scale = None
-    if case["kv"] == "fp8_e4m3":
-        live = (torch.arange(T, device=DEV) < st["n"].long()[:, None])[..., None, None]
-        scale = torch.stack([torch.clamp((x.float() * live).abs().amax((1, 3)),
-                                         min=2.0 ** -126) / 448.0 for x in (k, v)], -1)
-    if sealed is not None:
-        pick, whole, held = sealed
-        both = []
-        for x, name in ((k, "k"), (v, "v")):
-            rows = held[name].permute(0, 2, 1, 3).to(torch.bfloat16)
-            rows = torch.where(whole.permute(0, 2, 1)[..., None], rows, torch.gather(x, 1, pick))
-            both.append(x.scatter(1, pick, rows))
-        k, v = both
-        for name in ("store_k", "store_v", "ring_k", "ring_v", "length"):
-            del st[name]
-    c = _cache(case, case["Hq"], D, case["kv"], 0)
-    fd.fdms_append_evict(c, 0, B, st["n"], T, k, v, keep, kv_scale=scale)
-    fd.fdms_bounds_create(c)
-    st["cache"] = c
     return st
 
 
