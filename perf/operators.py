@@ -192,12 +192,7 @@ def _prepare_sparse(st, case, seed):
     st["out"] = torch.empty_like(st["q"])
     st["blocks"] = torch.empty((B, H, case["blocks"]), dtype=torch.int32, device=DEV)
     if own:
-        import compressed_decode_attention_fdms_b200 as fd
-        c = _cache(case, case["Hq"], D, case["kv"], 0)
-        fd.fdms_append_evict(c, 0, B, st["n"], T, k, v, keep)
-        fd.fdms_bounds_create(c)
-        st["cache"] = c
-        return st
+        return _fill(st, case, seed, k, v, keep)
     n = st["n"].long()[:, None, None]
     pos = torch.arange(T, device=DEV)[None, :, None]
     inside = pos < n
@@ -243,6 +238,48 @@ def _prepare_sparse(st, case, seed):
     kb = scaled["k"][:, :, :nb * BLOCK].unflatten(2, (nb, BLOCK)) if nb else \
         scaled["k"][:, :, :0].reshape(B, H, 0, BLOCK, D)
     st["kmin"], st["kmax"] = kb.amin(3), kb.amax(3)
+    return st
+
+
+def _fill(st, case, seed, k, v, keep):
+    """The calls' cache, with what the plain form's store holds.
+
+    A division of a GPU tensor by a number is a product with the number's rounded
+    reciprocal, so that the plain form's E4M3 scales are one unit off the cache's
+    quotients for some maxima, and a code next to a border can be another one. The
+    calls are measured on the plain form's values all the same: a cache with a scale
+    per head is given the scales; to one with a scale per block the rows of its full
+    blocks come as the values their codes stand for (in bf16, which is 2^-9 of the
+    value at most: they round to the same codes again)."""
+    global own
+    import compressed_decode_attention_fdms_b200 as fd
+    B, T, H, D = k.shape
+    n, scale = st["n"].long()[:, None, None], None
+    pos = torch.arange(T, device=DEV)[None, :, None]
+    if case["kv"] == "fp8_e4m3":
+        scale = torch.stack([torch.clamp((x.float() * (pos < n)[..., None]).abs().amax((1, 3)),
+                                         min=2.0 ** -126) / 448.0 for x in (k, v)], -1)
+    elif case["kv"] == "fp8_e4m3_block":
+        own = False
+        try:
+            held = _prepare_sparse({"n": st["n"]}, case, seed)
+        finally:
+            own = True
+        room = held["store_k"].shape[2]
+        stored = (pos < n - case["W"]) & (keep > 0)
+        order = torch.argsort((~stored).to(torch.uint8), dim=1, stable=True)
+        pick = order[:, :room, :, None].expand(-1, -1, -1, D)
+        full = torch.arange(room, device=DEV)[:, None] < (held["length"] // BLOCK * BLOCK)[:, None]
+        both = []
+        for x, name in ((k, "k"), (v, "v")):
+            rows = held["store_" + name].permute(0, 2, 1, 3).to(torch.bfloat16)
+            rows = torch.where(full[..., None], rows, torch.gather(x, 1, pick))
+            both.append(x.scatter(1, pick, rows))
+        k, v = both
+    c = _cache(case, case["Hq"], D, case["kv"], 0)
+    fd.fdms_append_evict(c, 0, B, st["n"], T, k, v, keep, kv_scale=scale)
+    fd.fdms_bounds_create(c)
+    st["cache"] = c
     return st
 
 
