@@ -196,6 +196,18 @@ __device__ __forceinline__ uint32_t low_bits(int k) {
   return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
 }
 
+// A row's sum of weights 2^(score - ref), once it passes 2^24, to between 1 and 4: the
+// reference rises by the sum's exponent. What its results are to be scaled by. (An
+// infinite sum stays, and so does NaN.)
+__device__ __forceinline__ float raise_ref(float& l, float& ref) {
+  if (!(l > 16777216.f)) return 1.f;
+  const int k = min((int)(__float_as_uint(l) >> 23) - 127, 126);
+  const float up = __uint_as_float((unsigned)(127 - k) << 23);   // 2^-k
+  ref += (float)k;
+  l *= up;
+  return up;
+}
+
 template <bool M>
 struct Masked {
   static constexpr bool value = M;
@@ -508,7 +520,9 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
       // tile that the row sees something of, and rises by the exponent of the row's sum
       // once that passes 2^24. (A tile that raises a weight past 2^127 at once makes
       // the row infinite, and it is computed again below. Maxima of every tile cost
-      // 800 of 3,700 cycles per key tile.)
+      // 800 of 3,700 cycles per key tile.) A split raises it once more at its end: the
+      // join weighs splits by their references, and a sum of 2^126 that the last tile
+      // brought would count for nothing beside a reference of 127.
       float ref = 0.f;
       bool has = false;       // a reference
       float l = 0.f;
@@ -556,13 +570,7 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
           }
           if (__any_sync(0xffffffffu, l > 16777216.f)) {
             // (x > 0) the sums so far are complete once the last product is
-            float up = 1.f;
-            if (l > 16777216.f) {
-              const int k = min((int)(__float_as_uint(l) >> 23) - 127, 126);
-              up = __uint_as_float((unsigned)(127 - k) << 23);   // 2^-k
-              ref += (float)k;
-              l *= up;
-            }
+            const float up = raise_ref(l, ref);
             ok = __all_sync(0xffffffffu, bar_wait(o_full + m, (done + x - 1) & 1, stop));
             if (!ok) break;
             tc_fence_after();
@@ -657,6 +665,7 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
         }
       } else {
         const long long at = (long long)it.split * a.batch * a.max_q * a.Hq + row;
+        const float up = raise_ref(l, ref);
         if (live) {
           a.part_ml[2 * at] = l == 0.f ? -INFINITY : ref;
           a.part_ml[2 * at + 1] = l;
@@ -667,6 +676,8 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
             uint32_t o[32];
             tmem_ld32(to + e, o);
             tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * up);
             if (live)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -1009,7 +1020,9 @@ k_prefill_few(const __grid_constant__ PrefillArgs a, int row_chunks, uint16_t* _
 
 // The partial results of a row's splits, joined: D / 4 lanes per row, eight CTAs per
 // block of rows (as the items of k_prefill_mma; what it costs is the chain of loads of
-// a warp's rows: one CTA per block took 29 us for 59k rows of two splits).
+// a warp's rows: one CTA per block took 29 us for 59k rows of two splits). A split's sum
+// is 2^38 at most and that of the largest reference 1 or more, so that one whose weight
+// becomes 0, with a reference 126 lower, has no share.
 template <int D>
 __global__ void __launch_bounds__(256)
 k_prefill_join(const __grid_constant__ PrefillArgs a, uint16_t* __restrict__ out,
