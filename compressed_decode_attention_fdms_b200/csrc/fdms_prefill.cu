@@ -81,7 +81,9 @@ __device__ __noinline__ void attend_row(const PrefillArgs& a, int b, int n, int 
       load_row<C>(a.v + at, lane, vx);
       const float s = dot<C>(qx, kx) * a.scale;
       const float m2 = fmaxf(m, s);
-      const float up = m2 == -INFINITY ? 1.f : __expf(m - m2), p = __expf(s - m2);
+      // (a score of -inf beside nothing else so far: a weight of 0, not exp(-inf + inf))
+      const float up = m2 == -INFINITY ? 1.f : __expf(m - m2);
+      const float p = m2 == -INFINITY && s == m2 ? 0.f : __expf(s - m2);
       l = l * up + p;
       for (int x = 0; x < C; ++x) o[x] = o[x] * up + p * vx[x];
       m = m2;
