@@ -57,7 +57,8 @@ __device__ __forceinline__ float dot(const float (&x)[C], const float (&y)[C]) {
 
 // One query row by one warp, token by token, touching only what it sees: the
 // rows whose tiles held infinities or NaN (a matrix product carries them into
-// rows that do not see them, as 0 * NaN).
+// rows that do not see them, as 0 * NaN), or whose sums passed what fp32 holds. The
+// result is kept as a mean of the V rows so far, which does not.
 template <int D>
 __device__ __noinline__ void attend_row(const PrefillArgs& a, int b, int n, int nq, int t, int h,
                                         uint16_t* out, float* lse) {
@@ -84,13 +85,16 @@ __device__ __noinline__ void attend_row(const PrefillArgs& a, int b, int n, int 
       // (a score of -inf beside nothing else so far: a weight of 0, not exp(-inf + inf))
       const float up = m2 == -INFINITY ? 1.f : __expf(m - m2);
       const float p = m2 == -INFINITY && s == m2 ? 0.f : __expf(s - m2);
-      l = l * up + p;
-      for (int x = 0; x < C; ++x) o[x] = o[x] * up + p * vx[x];
+      const float l2 = l * up + p;
+      if (l2 != 0.f) {
+        const float a0 = l * up / l2, a1 = p / l2;
+        for (int x = 0; x < C; ++x) o[x] = o[x] * a0 + vx[x] * a1;
+      }
+      l = l2;
       m = m2;
     }
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  for (int x = 0; x < C; ++x) out[row * D + lane * C + x] = f32_to_bf16_rn(o[x] * inv);
+  for (int x = 0; x < C; ++x) out[row * D + lane * C + x] = f32_to_bf16_rn(o[x]);
   if (lse && lane == 0) lse[row] = m + logf(l);
 }
 

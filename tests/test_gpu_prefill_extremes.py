@@ -1,6 +1,6 @@
 """Prompt attention where the parts of a row's keys differ by all that fp32 holds:
 splits whose sums come from a late jump, rows computed a second time whose first
-key has a score of -inf."""
+key has a score of -inf, values near the end of the range."""
 import numpy as np
 import pytest
 import torch
@@ -55,4 +55,19 @@ def test_first_key_of_minus_infinity_in_rows_computed_again(T, qs, D):
     o, z, tol, ztol = (x[rows] for x in c.reference(0))
     assert (np.abs(f64(c.out)[0, rows] - o) <= tol).all()
     assert (np.abs(f64(c.lse)[0, rows] - z) <= ztol).all()
+    c.check_error()
+
+
+@pytest.mark.parametrize("T,qs", [(300, None), (700, None), (2100, [7])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_near_the_end_of_the_range(T, qs, D):
+    """Sums of V rows pass what fp32 holds, their weighted means do not."""
+    c = Call([T], qs, 4, 2, D, W=T, seed=43, spread=0.2)
+    c.v[..., 1] = 2.0 ** 127
+    c.v[..., 2] = -(2.0 ** 126)
+    c.v[:, ::2, :, 3] = 2.0 ** 127
+    c.v[:, 1::2, :, 3] = -(2.0 ** 127)
+    c.attn()
+    torch.cuda.synchronize()
+    c.check_attn()
     c.check_error()
