@@ -24,14 +24,15 @@ LIB_PATH = os.path.join(HERE, "libfdms.so")
 FDMS_OK, FDMS_ERR_INVALID_ARG, FDMS_ERR_OUT_OF_BLOCKS, FDMS_ERR_CUDA, \
     FDMS_ERR_UNSUPPORTED, FDMS_ERR_DEVICE = range(6)
 FDMS_KV_BF16, FDMS_KV_FP8_E4M3, FDMS_KV_FP8_E4M3_BLOCK = 0, 1, 2
+FDMS_FOR_ATTN, FDMS_FOR_SCORES, FDMS_WITH_KEEP = 1, 2, 4
 
 # every symbol include/fdms.h declares
 EXPORTED = (
     "fdms_status_string", "fdms_cache_create", "fdms_cache_destroy", "fdms_append_evict",
     "fdms_decode_attn", "fdms_decode_attn_f32", "fdms_cache_stats", "fdms_cache_read_head",
     "fdms_decode_attn_noalloc", "fdms_decode_layout",
-    "fdms_prefill_workspace", "fdms_prefill_attn", "fdms_prefill_scores", "fdms_select_keep",
-    "fdms_bounds_create", "fdms_decode_attn_sparse",
+    "fdms_prefill_workspace", "fdms_prefill_workspace_for", "fdms_prefill_attn",
+    "fdms_prefill_scores", "fdms_select_keep", "fdms_bounds_create", "fdms_decode_attn_sparse",
 )
 
 
@@ -109,6 +110,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     Z = ctypes.c_size_t
     lib.fdms_prefill_workspace.restype = I
     lib.fdms_prefill_workspace.argtypes = [P, I, I, I, ctypes.POINTER(Z)]
+    lib.fdms_prefill_workspace_for.restype = I
+    lib.fdms_prefill_workspace_for.argtypes = [P, I, I, I, I, ctypes.POINTER(Z)]
     lib.fdms_prefill_attn.restype = I
     lib.fdms_prefill_attn.argtypes = [P, I, P, I, P, I, P, P, P, P, P, P, P, Z, P]
     lib.fdms_prefill_scores.restype = I
@@ -316,10 +319,21 @@ def fdms_cache_read_head(cache: Cache, layer: int, seq: int, kv_head: int, strea
 
 def fdms_prefill_workspace(cache: Cache, batch: int, max_n: int, max_q: int) -> int:
     """Bytes of workspace for fdms_prefill_attn / fdms_prefill_scores calls of up to
-    this batch, max_n and max_q (q.shape[1])."""
+    this batch, max_n and max_q (q.shape[1]), with keep bits or without."""
     n = ctypes.c_size_t()
     _check(load_library().fdms_prefill_workspace(cache.handle, batch, max_n, max_q,
                                                  ctypes.byref(n)), "fdms_prefill_workspace")
+    return n.value
+
+
+def fdms_prefill_workspace_for(cache: Cache, batch: int, max_n: int, max_q: int,
+                               uses: int) -> int:
+    """The same for calls of one kind: an OR of FDMS_FOR_ATTN, FDMS_FOR_SCORES and, if
+    they bring keep bits, FDMS_WITH_KEEP."""
+    n = ctypes.c_size_t()
+    _check(load_library().fdms_prefill_workspace_for(cache.handle, batch, max_n, max_q, uses,
+                                                     ctypes.byref(n)),
+           "fdms_prefill_workspace_for")
     return n.value
 
 

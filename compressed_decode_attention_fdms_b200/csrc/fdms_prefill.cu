@@ -1540,7 +1540,8 @@ struct Plan {
   int words;
   int key_tiles, chunks, chunk_steps;   // scores
   size_t off_bits, off_before, off_kc, off_vc, off_pos, off_o, off_ml, off_few, off_part;
-  size_t bytes;   // enough for this call and for every smaller one
+  // of workspace, enough for this call and for every smaller one
+  size_t attn_bytes, score_bytes;
 };
 constexpr int kCompactMin = 1024;
 constexpr int kFewShort = 512;         // tokens of a short prompt (most_few is 1)
@@ -1549,7 +1550,7 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 long long least_of(long long a, long long b) { return a < b ? a : b; }
 long long most_of(long long a, long long b) { return a > b ? a : b; }
 
-Plan plan_of(const fdms_cache* c, int batch, int max_n, int max_q) {
+Plan plan_of(const fdms_cache* c, int batch, int max_n, int max_q, bool keep) {
   const CacheView& v = c->view;
   Plan p = {};
   const long long heads = (long long)batch * v.Hkv, rows = (long long)batch * max_q * v.Hq;
@@ -1584,7 +1585,7 @@ Plan plan_of(const fdms_cache* c, int batch, int max_n, int max_q) {
   p.chunks = steps > 0 ? (int)ceil_div(steps, cs) : 1;
   // layout: the kept tokens, then either the attention's V rows and partial
   // results or the scores' positions and partial sums
-  p.compact = max_n >= kCompactMin && v.W < max_n;
+  p.compact = keep && max_n >= kCompactMin && v.W < max_n;
   p.words = (int)ceil_div(max_n, 32);
   const int kinds = p.compact ? 2 : 1;
   size_t at = 0;
@@ -1613,11 +1614,12 @@ Plan plan_of(const fdms_cache* c, int batch, int max_n, int max_q) {
   const long long sums =
       least_of(ceil_div(steps, 8) * base, most_of(12 * room + base, ceil_div(steps, 32) * base)) *
       kinds * kKeys;
+  if (max_q == 0) return p;
+  // (so few rows of a head that every smaller call has few too: nothing is compacted)
   const size_t few_end = up(frow * v.D * 4) + up(frow * 8);
-  size_t o_end = p.off_o + up(prow * v.D * 4) + up(prow * 8);
-  if (o_end < few_end) o_end = few_end;
-  const size_t s_end = p.off_part + (p.compact || steps > 8 ? up(sums * 4) : 0);
-  p.bytes = max_q == 0 ? 0 : o_end > s_end ? o_end : s_end;
+  const size_t o_end = p.off_o + up(prow * v.D * 4) + up(prow * 8);
+  p.attn_bytes = head_rows <= 2 * kFewRows || o_end < few_end ? few_end : o_end;
+  p.score_bytes = p.off_part + (p.compact || steps > 8 ? up(sums * 4) : 0);
   return p;
 }
 
@@ -1669,7 +1671,7 @@ fdms_status attn(fdms_cache* c, PrefillArgs a, const Plan& p, uint8_t* ws, uint1
                          {D, (long long)a.Hkv * D, T * a.Hkv * D}, 1, kKeys);
   maps.kc = maps.k;
   maps.vc = maps.v;
-  if (p.compact && a.keep) {
+  if (p.compact) {
     a.compact = 1;
     a.words = p.words;
     a.bits = reinterpret_cast<uint32_t*>(ws + p.off_bits);
@@ -1715,7 +1717,7 @@ fdms_status scores(fdms_cache* c, PrefillArgs a, const Plan& p, uint8_t* ws, con
             fdms_tensor_map(&maps.k, a.k, {D, a.Hkv, T, B},
                             {D, (long long)a.Hkv * D, T * a.Hkv * D}, 1, kKeys);
   maps.kc = maps.k;
-  if (p.compact && a.keep) {
+  if (p.compact) {
     a.compact = 1;
     a.words = p.words;
     a.bits = reinterpret_cast<uint32_t*>(ws + p.off_bits);
@@ -1808,15 +1810,25 @@ fdms_status fdms_prefill_setup(fdms_cache* c) {
   return (c->view.D == 64 ? setup<64>() : setup<128>()) ? FDMS_OK : FDMS_ERR_CUDA;
 }
 
-extern "C" fdms_status fdms_prefill_workspace(fdms_cache* c, int batch, int max_n, int max_q,
-                                              size_t* bytes_out) {
+extern "C" fdms_status fdms_prefill_workspace_for(fdms_cache* c, int batch, int max_n, int max_q,
+                                                  int uses, size_t* bytes_out) {
   if (!c || !bytes_out) return FDMS_ERR_INVALID_ARG;
   *bytes_out = 0;
   if (batch < 0 || batch > c->view.Bmax || max_n < 0 || max_n > c->view.max_seq_len ||
-      max_q < 0 || max_q > max_n)
+      max_q < 0 || max_q > max_n ||
+      (uses & ~(FDMS_FOR_ATTN | FDMS_FOR_SCORES | FDMS_WITH_KEEP)))
     return FDMS_ERR_INVALID_ARG;
-  *bytes_out = plan_of(c, batch, max_n, max_q).bytes;
+  const Plan p = plan_of(c, batch, max_n, max_q, uses & FDMS_WITH_KEEP);
+  const size_t attn = uses & FDMS_FOR_ATTN ? p.attn_bytes : 0;
+  const size_t scores = uses & FDMS_FOR_SCORES ? p.score_bytes : 0;
+  *bytes_out = attn > scores ? attn : scores;
   return FDMS_OK;
+}
+
+extern "C" fdms_status fdms_prefill_workspace(fdms_cache* c, int batch, int max_n, int max_q,
+                                              size_t* bytes_out) {
+  return fdms_prefill_workspace_for(c, batch, max_n, max_q,
+                                    FDMS_FOR_ATTN | FDMS_FOR_SCORES | FDMS_WITH_KEEP, bytes_out);
 }
 
 extern "C" fdms_status fdms_prefill_attn(fdms_cache* c, int batch, const int32_t* n_dev, int max_n,
@@ -1830,8 +1842,9 @@ extern "C" fdms_status fdms_prefill_attn(fdms_cache* c, int batch, const int32_t
   if (batch == 0 || max_q == 0) return FDMS_OK;
   if (!v_dev || !out_dev || (((uintptr_t)v_dev | (uintptr_t)out_dev) & 15))
     return FDMS_ERR_INVALID_ARG;
-  const Plan p = plan_of(c, batch, max_n, max_q);
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)))
+  const Plan p = plan_of(c, batch, max_n, max_q, keep_dev != nullptr);
+  if (p.attn_bytes > 0 &&
+      (!workspace || workspace_bytes < p.attn_bytes || ((uintptr_t)workspace & 255)))
     return FDMS_ERR_INVALID_ARG;
   fdms_device_guard guard(c->device);
   const PrefillArgs a =
@@ -1852,8 +1865,9 @@ extern "C" fdms_status fdms_prefill_scores(fdms_cache* c, int batch, const int32
   if (st != FDMS_OK) return st;
   if (batch == 0 || max_n == 0) return FDMS_OK;
   if (!scores_dev || (max_q > 0 && !lse_dev)) return FDMS_ERR_INVALID_ARG;
-  const Plan p = plan_of(c, batch, max_n, max_q);
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)))
+  const Plan p = plan_of(c, batch, max_n, max_q, keep_dev != nullptr);
+  if (p.score_bytes > 0 &&
+      (!workspace || workspace_bytes < p.score_bytes || ((uintptr_t)workspace & 255)))
     return FDMS_ERR_INVALID_ARG;
   fdms_device_guard guard(c->device);
   const PrefillArgs a =

@@ -310,15 +310,27 @@ fdms_status fdms_cache_read_head(fdms_cache* cache, int layer, int seq, int kv_h
  * finite is computed a second time, token by token: results as defined, but slow (a
  * prompt of 8K tokens with NaN in every one: 0.3 s; over a million such tokens may
  * run into the bound and latch DEVICE).
- *   workspace  fdms_prefill_workspace bytes of device memory, 256-byte aligned,
- *            the call's own until its work on the stream is done (calls that may
- *            overlap on the GPU, two captured graphs included, need one each);
- *            may be NULL when that size is 0. Its contents need not be kept. */
+ *   workspace  fdms_prefill_workspace_for bytes of device memory (or more),
+ *            256-byte aligned, the call's own until its work on the stream is done
+ *            (calls that may overlap on the GPU, two captured graphs included, need
+ *            one each); may be NULL when that size is 0. Its contents need not be
+ *            kept. */
 
 #define FDMS_MAX_PROMPT (1 << 30)
 
-/* Bytes of workspace that fdms_prefill_attn and fdms_prefill_scores want for
- * calls of up to this batch, max_n and max_q on this cache. */
+/* What a workspace is to serve: fdms_prefill_attn, fdms_prefill_scores, calls that
+ * bring keep bits (keep_dev not NULL; from 1024 tokens on the kept tokens' K rows,
+ * and for the attention of more than 64 query rows per kv head V rows, are copied
+ * to it). */
+enum { FDMS_FOR_ATTN = 1, FDMS_FOR_SCORES = 2, FDMS_WITH_KEEP = 4 };
+
+/* Bytes of workspace for calls of up to this batch, max_n and max_q on this cache.
+ *   uses  an OR of the above. A call is refused (INVALID_ARG) if its workspace is
+ *         smaller than what it wants for its own use and sizes. */
+fdms_status fdms_prefill_workspace_for(fdms_cache* cache, int batch, int max_n, int max_q,
+                                       int uses, size_t* bytes_out);
+
+/* The same for every use. */
 fdms_status fdms_prefill_workspace(fdms_cache* cache, int batch, int max_n, int max_q,
                                    size_t* bytes_out);
 
