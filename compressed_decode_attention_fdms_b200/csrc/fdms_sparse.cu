@@ -50,7 +50,7 @@ struct Sum {
   }
 };
 
-// score in the selection's order: NaN first
+// score in the selection's order: NaN as +infinity
 __device__ __forceinline__ double ranked(double u) { return u != u ? (double)INFINITY : u; }
 
 // a whole number in the order of the score (-0 and 0 equal)

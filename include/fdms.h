@@ -382,8 +382,8 @@ fdms_status fdms_select_keep(fdms_cache* cache, int batch, const int32_t* n_dev,
 fdms_status fdms_bounds_create(fdms_cache* cache, void* stream);
 
 /* fdms_decode_attn over part of the store: per (seq, kv head) the num_select full
- * blocks with the largest score (equal scores: the lower block; a NaN sum ranks
- * first), the partly filled last block and the ring. With num_select >= the full
+ * blocks with the largest score (equal scores: the lower block; a NaN sum counts as
+ * +infinity), the partly filled last block and the ring. With num_select >= the full
  * blocks it is fdms_decode_attn. Products of the score are exact, its sums to
  * about 2^-46 of their terms. The bounds are part of the cache's state: a call finds those
  * of blocks filled since the last one from their rows, once per block.
