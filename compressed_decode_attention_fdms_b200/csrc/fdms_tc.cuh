@@ -204,17 +204,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
-}
 // the same for 16 columns
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
@@ -330,8 +319,8 @@ __device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {
 // unit (4 results a cycle and SM quarter) holds up: x = r + f with r whole and
 // |f| <= 1/2, 2^f by a polynomial of degree 5 (least relative error over
 // [-1/2, 1/2], found by weighted least squares; 2.1e-7 with fp32 steps, as good
-// as the unit's), times 2^r put together in the exponent's bits: exact zeros
-// from -127 down, infinity from 128 up, NaN kept.
+// as the unit's), times 2^r put together in the exponent's bits: exact zeros where
+// r is -127 (x below -126.5), infinity where it is 128 (from 127.5 up), NaN kept.
 __device__ __forceinline__ float2 exp2_mad(float2 x) {
   const float big = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number
   x.x = clamp_nan(x.x, -127.f, 128.f);
