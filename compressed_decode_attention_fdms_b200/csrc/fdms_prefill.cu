@@ -534,9 +534,7 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
       // tile that the row sees something of, and rises by the exponent of the row's sum
       // once that passes 2^24. (A tile that raises a weight past 2^127 at once makes
       // the row infinite, and it is computed again below. Maxima of every tile cost
-      // 800 of 3,700 cycles per key tile.) A split raises it once more at its end: the
-      // join weighs splits by their references, and a sum of 2^126 that the last tile
-      // brought would count for nothing beside a reference of 127.
+      // 800 of 3,700 cycles per key tile.) What the last tile brought a split is left to the join.
       float ref = 0.f;
       bool has = false;       // a reference
       float l = 0.f;
@@ -679,7 +677,6 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
         }
       } else {
         const long long at = (long long)it.split * a.batch * a.max_q * a.Hq + row;
-        const float up = raise_ref(l, ref);
         if (live) {
           a.part_ml[2 * at] = l == 0.f ? -INFINITY : ref;
           a.part_ml[2 * at + 1] = l;
@@ -690,8 +687,6 @@ k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ Pre
             uint32_t o[32];
             tmem_ld32(to + e, o);
             tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * up);
             if (live)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -1034,10 +1029,12 @@ k_prefill_few(const __grid_constant__ PrefillArgs a, int row_chunks, uint16_t* _
 
 // The partial results of a row's splits, joined: D / 4 lanes per row, eight CTAs per
 // block of rows (as the items of k_prefill_mma; what it costs is the chain of loads of
-// a warp's rows: one CTA per block took 29 us for 59k rows of two splits). A split's sum
-// is 2^38 at most and that of the largest reference 1 or more, so that one whose weight
-// becomes 0, with a reference 126 lower, has no share.
-template <int D>
+// a warp's rows: one CTA per block took 29 us for 59k rows of two splits). A split's last
+// tile may have left a sum of up to 2^127 beside a low reference, which is raised first:
+// sums are small then (few rows', not TILES: 2^38) and that of the largest reference 1 or more, so
+// that a split whose weight becomes 0, with a reference 126 lower, has no share. (Raised
+// by the splits themselves: 2.5 us of 161 more for 8K tokens of heads of 64 with keep bits.)
+template <int D, bool TILES>
 __global__ void __launch_bounds__(256)
 k_prefill_join(const __grid_constant__ PrefillArgs a, uint16_t* __restrict__ out,
                float* __restrict__ lse) {
@@ -1051,7 +1048,7 @@ k_prefill_join(const __grid_constant__ PrefillArgs a, uint16_t* __restrict__ out
   int n, nq;
   if (!lengths(a, b, n, nq) || t0 >= nq) return;
   int splits = a.splits;
-  if (a.split_len > 0) {                    // (few rows: all of them)
+  if (TILES) {                              // (few rows: all of them)
     const int blocks = (a.max_q + TB - 1) / TB;
     splits = attn_item(a, ((blocks - 1 - t0 / TB) * BH + bh) * a.splits).splits;
     if (splits == 1) return;                // its rows are final
@@ -1063,22 +1060,29 @@ k_prefill_join(const __grid_constant__ PrefillArgs a, uint16_t* __restrict__ out
     const bool live = r < rows;
     const long long row = live ? ((long long)b * a.max_q + t) * a.Hq + h : 0;
     float m = -INFINITY;
-    for (int s = 0; live && s < splits; ++s) m = fmaxf(m, a.part_ml[2 * (s * all + row)]);
+    for (int s = 0; live && s < splits; ++s) {
+      float ref = a.part_ml[2 * (s * all + row)];
+      if (TILES) {
+        float sum = a.part_ml[2 * (s * all + row) + 1];
+        raise_ref(sum, ref);
+      }
+      m = fmaxf(m, ref);
+    }
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
       const long long at = s * all + row;
-      const float2 ml = live ? *reinterpret_cast<const float2*>(a.part_ml + 2 * at)
-                             : make_float2(-INFINITY, 0.f);
+      float2 ml = live ? *reinterpret_cast<const float2*>(a.part_ml + 2 * at)
+                       : make_float2(-INFINITY, 0.f);
       if (ml.y == 0.f) continue;            // nothing seen there (and no partial result)
       const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + sub * 4);
-      const float w = fast_exp2(ml.x - m);
+      const float up = TILES ? raise_ref(ml.y, ml.x) : 1.f, w = fast_exp2(ml.x - m);
       l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
+      o.x = fmaf(w, x.x * up, o.x);
+      o.y = fmaf(w, x.y * up, o.y);
+      o.z = fmaf(w, x.z * up, o.z);
+      o.w = fmaf(w, x.w * up, o.w);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     bool bad = !(l < INFINITY);
@@ -1656,7 +1660,7 @@ fdms_status attn(fdms_cache* c, PrefillArgs a, const Plan& p, uint8_t* ws, uint1
   const int TB = 2 * kRows / a.G;
   const long long blocks = (long long)a.batch * a.Hkv * ((a.max_q + TB - 1) / TB);
   a.splits = p.splits;
-  a.split_len = p.row_chunks ? 0 : p.split_len;
+  a.split_len = p.split_len;
   if (p.row_chunks) {
     // partial results from the workspace's start on
     a.part_o = reinterpret_cast<float*>(ws);
@@ -1665,8 +1669,8 @@ fdms_status attn(fdms_cache* c, PrefillArgs a, const Plan& p, uint8_t* ws, uint1
     auto few = one ? k_prefill_few<D, 1> : k_prefill_few<D, 2>;
     if (launch(few, dim3((unsigned)(a.batch * a.Hkv * p.row_chunks * p.splits)), kFewWarps * 32,
                FewL<D>::SMEM, s, a, p.row_chunks, out, lse) != cudaSuccess ||
-        (p.splits > 1 && launch(k_prefill_join<D>, dim3((unsigned)(blocks * 8)), 256, 0, s, a, out,
-                                lse) != cudaSuccess))
+        (p.splits > 1 && launch(k_prefill_join<D, false>, dim3((unsigned)(blocks * 8)), 256, 0, s,
+                                a, out, lse) != cudaSuccess))
       return FDMS_ERR_CUDA;
     return FDMS_OK;
   }
@@ -1707,7 +1711,7 @@ fdms_status attn(fdms_cache* c, PrefillArgs a, const Plan& p, uint8_t* ws, uint1
              lse) != cudaSuccess)
     return FDMS_ERR_CUDA;
   if (a.splits > 1) {
-    if (launch(k_prefill_join<D>, dim3((unsigned)(blocks * 8)), 256, 0, s, a, out,
+    if (launch(k_prefill_join<D, true>, dim3((unsigned)(blocks * 8)), 256, 0, s, a, out,
                lse) != cudaSuccess)
       return FDMS_ERR_CUDA;
   }
