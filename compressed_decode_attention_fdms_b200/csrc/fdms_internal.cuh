@@ -271,7 +271,6 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 
 }  // namespace fdms
 
-// Host-side cache object.
 // Block-sparse decode: key bounds and the selection it leaves for the decode
 // kernels (all NULL until fdms_bounds_create).
 namespace fdms {
@@ -288,6 +287,7 @@ struct SparseWork {
 };
 }  // namespace fdms
 
+// Host-side cache object.
 struct fdms_cache {
   fdms_config cfg;
   int device;

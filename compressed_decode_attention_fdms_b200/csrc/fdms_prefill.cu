@@ -292,12 +292,19 @@ __device__ __forceinline__ AttnItem attn_item(const PrefillArgs& a, int x) {
 // its place, in bf16: half the columns, and the form the second product wants) and O.
 // Rows of a kv head's group share K and V, so a tile of 128 rows spans 128 / G tokens.
 //
+// The weights enter the second product rounded to bf16 (one rounding, 2^-8 at most; 2.1e-3
+// off 64 bits in the 2-norm where rounding the result alone gives 1.6e-3): with a head and a
+// remainder, which decode carries, that product, half of the tensor work, would be done
+// twice. Sums and denominators are fp32.
+//
 // What bounds it: of 3,500 cycles per key tile and row tile pair the products take
 // 2,048 at heads of 128 (1,024 at 64) and the exponentials 2,048; neither is busy all
 // the time, since a tile's products and softmax follow one another and two tiles only
-// half cover the gaps. 8K tokens, 32/8 heads of 128, nothing evicted: 465 to 500 us,
-// 1.1 to 1.2 PFLOP/s of measured 1.66. With 5 to 30 % kept, heads of 64: 162 us,
-// of which the compaction is 9; two key tiles of three cover the window there.
+// half cover the gaps. 8K tokens, 32/8 heads of 128, nothing evicted: 550 us, 470 in a
+// burst of twenty passes: 1.00 and 1.17 PFLOP/s of measured 1.40 sustained, 1.66 in a
+// burst. With 5 to 30 % kept, heads of 64: 142 to 160 us by the keep rates drawn, of
+// which the compaction is 9; two key tiles of three cover the window there. The softmax
+// branch spills 76 bytes a thread (its 128 scores fill 208 registers).
 template <int D>
 __global__ void __launch_bounds__(AttnL<D>::THREADS, 1)
 k_prefill_mma(const __grid_constant__ PrefillArgs a, const __grid_constant__ PrefillMaps maps,
@@ -908,7 +915,7 @@ k_prefill_few(const __grid_constant__ PrefillArgs a, int row_chunks, uint16_t* _
           up[y] = 1.f;
           if (mx[r][y] == -INFINITY) {
             mx[r][y] = tm;
-          } else if ((tm - mx[r][y]) * sl2 > 8.f) {   // as in k_prefill_mma
+          } else if ((tm - mx[r][y]) * sl2 > 8.f) {   // weights stay under 2^8
             up[y] = fast_exp2((mx[r][y] - tm) * sl2);
             l[r][y] *= up[y];
             mx[r][y] = tm;
@@ -1555,8 +1562,18 @@ struct Plan {
   // of workspace, enough for this call and for every smaller one
   size_t attn_bytes, score_bytes;
 };
+// Tokens from which the kept ones are compacted. Compacted / masked in place, attention
+// of 32/8 heads of 64 with a fifth kept and a window of 256: 640 tokens 28 / 24 us, 1024
+// 39 / 36 (window of 16: 30 / 37), 2048 37 / 56, 4096 70 / 144; heads of 128 at 1024
+// 51 / 55. Fewer heads cross later (4/2 of 64: 2048 26 / 25, 4096 42 / 56), and so do the
+// scores (32/8 of 64: 1024 30 / 21, 2048 44 / 42, 4096 80 / 112).
 constexpr int kCompactMin = 1024;
-constexpr int kFewShort = 512;         // tokens of a short prompt (most_few is 1)
+// Tokens of a short prompt (most_few is 1), if its row chunks all run at once. By
+// k_prefill_few / in tiles, 4/2 heads of 64: 128 tokens 6.6 / 9.2 us, 256 8.3 / 11.0,
+// 512 11.7 / 14.1 (a quarter kept: 8.6 / 15.0), and beyond the rule still 768 15.3 / 19.7,
+// 1024 18.5 / 21. 32/8 heads fill the device at 256 tokens (heads of 64 10.0 / 11.1 us, of
+// 128 14.5 / 14.2) and go in tiles above.
+constexpr int kFewShort = 512;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 long long least_of(long long a, long long b) { return a < b ? a : b; }
@@ -1588,7 +1605,11 @@ Plan plan_of(const fdms_cache* c, int batch, int max_n, int max_q, bool keep) {
     p.splits = (int)(want < 1 ? 1 : want < most_few ? want : most_few);
   }
   // scores: chunks of 8 to 32 steps of 128 query rows, six items or more (half of
-  // the chunks are empty) for each of the two CTAs per SM
+  // the chunks are empty) for each of the two CTAs per SM. A chunk more is a plane of
+  // partial sums more, and a join. At least 8 / 4 / 2 steps: 4/2 heads of 64, 512 tokens
+  // 11.0 / 9.6 / 8.2 us, 1024 13.2 / 9.9 / 8.6; 32/8 heads, 512 13.7 / 10.3 / 10.3, 768
+  // 14.4 / 14.0 / 14.6, 1024 18.7 / 19.7 / 17.8 (of 128: 20.0 / 21.4 / 19.2): 8 is not the
+  // best for short prompts.
   const long long steps = ceil_div(max_q, kRows / v.G), base = heads * tiles;
   long long cs = ceil_div(base * steps, 12 * room);
   cs = cs < 8 ? 8 : cs > 32 ? 32 : cs;

@@ -11,9 +11,11 @@
 // to shared memory as a whole where they fit (up to kStage tokens): what bounds
 // the kernel is the latency of one head's passes, and with four loads under way
 // per thread reading them from L2 took 38.5 us for 256 heads of up to 32K tokens.
-// Now 30 us (23.7 MB, 3.6 us at the memory's rate): a head of 32K tokens takes 20 us, of
+// Now 28.5 us (23.7 MB, 3.6 us at the memory's rate): a head of 32K tokens takes 20 us, of
 // which the histogram is 4, the gather 4 and the bits 6 (bytes in every Hkv-th place,
-// 1.2 M partial sectors in all), and 256 of them take two rounds of the SMs.
+// 1.2 M partial sectors in all), and 256 of them take two rounds of the SMs. Heads above
+// kStage read their scores from L2 in each pass: 77 us for eight heads of 128K tokens,
+// and for 64 of them too.
 #include "fdms_tc.cuh"
 
 using namespace fdms;
